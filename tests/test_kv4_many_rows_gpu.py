@@ -1,0 +1,74 @@
+"""The many-row attention over the 4-bit cache (more than 16 rows of a head and
+sequence, heads of 64 and 128) where its own paths can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv4_ref
+from tests.gpu_util import bf16_to_dev, dev
+from tests.test_kv4_gpu import Step, _no_error, wq  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def _codes(st, value, b, h, keys, codes):
+    """Sets the codes of some of a sequence's keys (or values), leaving their scales."""
+    n = st.page * st.D // 2
+    for j in keys:
+        blk = st.pool[st.table[b, j // st.page], h]
+        row = np.zeros(st.D // 8, dtype=np.uint32)
+        place = kv4_ref.value_place if value else kv4_ref.key_place
+        for d in range(st.D):
+            w, nib = place(st.D, d)
+            row[w] |= np.uint32(int(codes[d]) + 8) << np.uint32(4 * nib)
+        at = value * n + j % st.page * st.D // 2
+        blk[at:at + st.D // 2] = row.astype("<u4").view(np.uint8)
+
+
+def _scales(st, value, b, h, keys, scale):
+    n, G = st.page * st.D // 2, st.D // st.group
+    for j in keys:
+        s = st.pool[st.table[b, j // st.page], h][2 * n + value * st.page * 2 * G:][:st.page * 2 * G]
+        s.view("<u2").reshape(st.page, G)[j % st.page] = kv4_ref.bf16(np.float32(scale))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens", [10, 60])           # 40 rows (one tile), 240 (two)
+@pytest.mark.parametrize("per_key", [False, True])     # keys that share their factors, and keys that do not
+@pytest.mark.parametrize("column", [5, 40, 70, 100, 127])
+def test_a_larger_score_late_in_a_block(wq, D, tokens, per_key, column):  # noqa: F811
+    """Keys of equal weight, but one in the third block of 128 that weighs 2^10.8 as much: the reference moves while
+    the weights of the block's earlier pieces are on their way, and the other keys together still are a tenth of the
+    result.  160 sequences that share their pages, so that a CTA has several of an item's blocks."""
+    B = 160
+    st = Step(wq, [tokens], [128 * 3 + tokens], D=D, group=D, page=32, Hkv=1, seed=column)
+    m = st.kv[0]
+    rng = np.random.default_rng(column + tokens)
+    half = np.arange(D) % 2 * 2 - 1
+    for j in range(m):
+        # opposite codes in neighbouring dimensions: nothing of a query that is the same in all dimensions
+        _codes(st, 0, 0, 0, [j], np.repeat(rng.integers(-7, 8, size=D // 2), 2) * half)
+    _scales(st, 0, 0, 0, range(m), 2.0 ** -6)
+    late = 256 + column
+    _codes(st, 0, 0, 0, [late], np.ones(D))
+    _scales(st, 0, 0, 0, [late], 1.0)
+    _scales(st, 1, 0, 0, range(m), 0.25)
+    if per_key:  # within a warp's sixteen keys, further apart than 2^12
+        _scales(st, 0, 0, 0, [3, 131, 259, 258 + 64], 2.0 ** -20)
+    st.upload(wq)
+    base = 10.8 * np.log(2) / D ** 0.5
+    bits = kv4_ref.bf16(base * np.ones((tokens, 4, D)) + rng.normal(size=(tokens, 4, D)) * 2.0 ** -10)
+    Q = kv4_ref.widen(bits).reshape(tokens, 4, D)
+    batch = wq.kv4_batch(st.batch.page_table.expand(B, -1).contiguous(),
+                         torch.arange(B + 1, dtype=torch.int32, device=dev()) * tokens,
+                         torch.full((B,), m, dtype=torch.int32, device=dev()), B * tokens, max_q=tokens)
+    queries = bf16_to_dev(bits).view(1, tokens, 4, D).expand(B, -1, -1, -1).reshape(B * tokens, 4, D)
+    O = wq.kv4_attention(queries, st.cache, batch)
+    assert torch.equal(O, wq.kv4_attention(queries, st.cache, batch))
+    got = O.float().cpu().numpy().astype(np.float64).reshape(B, tokens, 4, D)
+    K, V = st.keys_values(0, 0)
+    pos = np.arange(m - tokens, m)
+    for h in range(4):
+        ref, A, big = kv4_ref.attention(Q[:, h], K, V, pos, D ** -0.5, 0)
+        tol = kv4_ref.many_row_tolerance(ref, A, big, Q[:, h], K, V, pos, D ** -0.5, 0)
+        assert (np.abs(got[:, :, h] - ref) <= tol).all(), (h, float((np.abs(got[:, :, h] - ref) / tol).max()))

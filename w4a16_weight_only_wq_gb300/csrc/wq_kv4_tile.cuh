@@ -286,6 +286,7 @@ static __device__ __noinline__ float first_reference(uint32_t ts, const float* k
 // What a row has so far times f, a power of two of 1 or less: the weights in
 // `wcols` columns at ts and O's `ocols` at to.
 static __device__ __noinline__ void shrink(uint32_t ts, int wcols, uint32_t to, int ocols, float f) {
+  tmem_st_wait();  // the pieces' weights have been stored without a wait, and a load does not wait for stores
 #pragma unroll 1
   for (int q = 0; q < wcols; q += 8) {
     uint32_t v[8];
