@@ -827,12 +827,16 @@ kv4_tile_kernel(const TileParams tp) {
       n_block += n;
       u = it.start + x1;
     }
-    // after giving up: let what was issued finish before tensor memory goes
-    if (issuer && lane == 0 && *abort_flag) {
-      umma_commit(&mma_done[stream]);
-      KernelDiag d = tp.diag;
-      if (d.wait_limit_ns < 1000000000ull) d.wait_limit_ns = 1000000000ull;
-      mbar_wait_bounded(&mma_done[stream], 0, d);
+    // after giving up: let what was issued finish before tensor memory goes (a
+    // commit counts its own thread's products, so the lane that issued them waits)
+    if (issuer && __any_sync(0xffffffffu, *abort_flag)) {
+      if (elect_one()) {
+        umma_commit(&mma_done[stream]);
+        KernelDiag d = tp.diag;
+        if (d.wait_limit_ns < 1000000000ull) d.wait_limit_ns = 1000000000ull;
+        mbar_wait_bounded(&mma_done[stream], 0, d);
+      }
+      __syncwarp();
     }
   } else {
     // ================================================= codes to operands
