@@ -361,8 +361,9 @@ WQ_API wq_status wq_kv4_read(const wq_kv4_cache* cache, const wq_kv4_batch* batc
 
 /* Bytes of the attention's workspace for Hq query heads; 0 for unsupported
    arguments.  It does not depend on the batch.  The workspace must hold
-   zeros before its first use; every call leaves it fit for the next one on
-   the same stream.  Two streams need one each.  Host arithmetic (it asks the
+   zeros before its first use; every call, also one that a wait which ran out
+   has ended, leaves it fit for the next one on the same stream.  Two streams
+   need one each.  Host arithmetic (it asks the
    current device for its SM count; 152 where there is none). */
 WQ_API size_t wq_kv4_workspace_bytes(int64_t Hq, int Hkv, int D);
 
@@ -442,9 +443,10 @@ WQ_API const char* wq_last_cuda_error(void);
    wq_debug_force_timeout(mode): 0 off; 1 every CTA of the next GEMMs first
    waits on a barrier nothing completes -- the wait runs out, is reported,
    and the GEMM then runs normally; 2 the data waits look for a phase that
-   never completes, so the GEMM gives up, lets its copies land and reports
-   (its output is then undefined).  Both report WQ_ERR_DEVICE_TIMEOUT
-   through wq_last_device_error() without any fault. */
+   never completes, so the GEMM (or wq_kv4_attention of more than 16 rows)
+   gives up, lets its copies and products finish and reports (its output is
+   then undefined).  Both report WQ_ERR_DEVICE_TIMEOUT through
+   wq_last_device_error() without any fault. */
 WQ_API void wq_debug_set_wait_limit_ns(uint64_t ns);
 WQ_API void wq_debug_force_timeout(int mode);
 

@@ -72,3 +72,33 @@ def test_a_larger_score_late_in_a_block(wq, D, tokens, per_key, column):  # noqa
         ref, A, big = kv4_ref.attention(Q[:, h], K, V, pos, D ** -0.5, 0)
         tol = kv4_ref.many_row_tolerance(ref, A, big, Q[:, h], K, V, pos, D ** -0.5, 0)
         assert (np.abs(got[:, :, h] - ref) <= tol).all(), (h, float((np.abs(got[:, :, h] - ref) / tol).max()))
+
+
+def test_a_wait_that_runs_out_leaves_the_workspace_fit(wq):  # noqa: F811
+    """Items shared by CTAs, a CTA's range ending inside one it has not reached when it gives up; the same workspace
+    afterwards, for this kernel and for the few-row one."""
+    st = Step(wq, [16, 16, 16], [20000, 20000, 1000], D=128, group=128, page=256, Hkv=4, seed=40)
+    one = wq.kv4_batch(st.batch.page_table, torch.arange(4, dtype=torch.int32, device=dev()), st.batch.kv_len, 3, max_q=1)
+    ws = wq.kv4_workspace(16, st.cache)
+    bits = kv4_ref.bf16(np.random.default_rng(41).normal(size=(st.T, 16, 128)))
+    Q = bf16_to_dev(bits).view(st.T, 16, 128)
+
+    def both():
+        return (wq.kv4_attention(Q, st.cache, st.batch, workspace=ws),
+                wq.kv4_attention(Q[:3], st.cache, one, workspace=ws))
+
+    want = both()
+    try:
+        wq.wq_debug_set_wait_limit_ns(20_000_000)
+        wq.wq_debug_force_timeout(2)
+        both()
+        torch.cuda.synchronize()
+        assert wq.wq_last_device_error() == wq.WQ_ERR_DEVICE_TIMEOUT
+    finally:
+        wq.wq_debug_force_timeout(0)
+        wq.wq_debug_set_wait_limit_ns(0)
+        wq.wq_clear_device_error()
+    counters = ws[:2048]  # of 608 CTAs
+    assert not counters.any()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, both()))

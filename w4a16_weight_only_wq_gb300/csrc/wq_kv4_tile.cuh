@@ -172,6 +172,29 @@ __device__ __forceinline__ int64_t seq_units(const Params& p, int b) {
   return sum * p.kv.Hkv;
 }
 
+// A CTA that gives up in the item that holds unit u still counts as arrived at
+// the one item that it has not reached and that others share, the last of its
+// range: so the counters are zeros again when all CTAs are through.  `scan`: the
+// units before each chunk of sequences.
+template <int kRows, int kChunks>
+static __device__ __noinline__ void arrive_at_last(const Params& p, const int64_t* scan, int64_t u) {
+  const int64_t U = scan[kChunks], C = U < gridDim.x ? U : gridDim.x, cta = blockIdx.x;
+  const int64_t u1 = U * (cta + 1) / C;  // where the CTA's range ends
+  int lo = 0, hi = kChunks;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (scan[mid] < u1) lo = mid; else hi = mid;
+  }
+  Walk<kRows> walk(p);
+  walk.open(lo * ((p.kv.B + kChunks - 1) / kChunks), scan[lo]);
+  walk.seek(u1 - 1);
+  const int64_t end = walk.it.start + walk.it.units;
+  if (walk.it.start <= u || end <= u1) return;  // (has been reached; or is this CTA's alone)
+  int64_t last = (end - 1) * C / U;  // the CTA that has the item's last unit
+  while (U * (last + 1) / C < end) ++last;
+  if (atomicAdd(p.arrived + cta, 1u) == static_cast<uint32_t>(last - cta)) p.arrived[cta] = 0;
+}
+
 // ------------------------------------------------------------ fp16 pairs ---
 // Two fp32 numbers in one register pair, and their instructions.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -684,7 +707,8 @@ kv4_tile_kernel(const TileParams tp) {
     };
     int64_t n_block = 0;              // blocks of the CTA so far (the factors' ring)
     bool ok = true;                   // no wait of this warp has given up
-    for (int64_t u = u0; u < u1;) {
+    int64_t u = u0;
+    while (u < u1) {
       walk.seek(u);
       const Item& it = walk.it;
       const int x0 = static_cast<int>(u - it.start), x1 = static_cast<int>(min(it.start + it.units, u1) - it.start);
@@ -827,6 +851,7 @@ kv4_tile_kernel(const TileParams tp) {
       n_block += n;
       u = it.start + x1;
     }
+    if (tid == 0 && u < u1) arrive_at_last<kRows, kThreads>(p, s_scan, u);
     // after giving up: let what was issued finish before tensor memory goes (a
     // commit counts its own thread's products, so the lane that issued them waits)
     if (issuer && __any_sync(0xffffffffu, *abort_flag)) {
