@@ -394,8 +394,10 @@ WQ_API wq_status wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_batch*
                                   int64_t window, void* workspace, size_t workspace_bytes,
                                   cudaStream_t stream);
 
-/* Bytes of wq_token_logprobs' workspace; 0 for unsupported arguments.  Zeros
-   before its first use, one stream at a time, as wq_kv4_workspace_bytes. */
+/* Bytes of wq_token_logprobs' workspace for any call of up to T rows of up to
+   V logits with up to k alternatives, of either type; 0 for unsupported
+   arguments.  Zeros before its first use, one stream at a time; every call
+   leaves it fit for the next one, whatever that one's sizes. */
 WQ_API size_t wq_logprobs_workspace_bytes(int64_t T, int64_t V, int k);
 
 /*

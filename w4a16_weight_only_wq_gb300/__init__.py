@@ -608,7 +608,8 @@ def kv4_attention(Q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, scale: floa
 
 # ------------------------------------------- log probabilities of tokens ---
 def logprobs_workspace(T: int, V: int, k: int = 0, device="cuda") -> torch.Tensor:
-    """``token_logprobs``' workspace for T rows of V logits and k alternatives: one per stream."""
+    """``token_logprobs``' workspace for up to T rows of up to V logits and up to k alternatives: one per stream, for
+    calls of any such sizes."""
     n = wq_logprobs_workspace_bytes(T, V, k)
     if n == 0:
         raise WQError(WQ_ERR_SHAPE, "logprobs_workspace")

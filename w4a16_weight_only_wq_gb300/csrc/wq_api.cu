@@ -656,7 +656,6 @@ wq_status wq_token_logprobs(const void* logits, wq_dtype dt, int64_t T, int64_t 
   DeviceInfo d;
   const wq_status st = device_info(&dev, &d);
   if (st != WQ_OK) return st;
-  if (workspace_bytes < wq::logprobs_workspace_bytes(T, V, k, d.num_sms)) return WQ_ERR_SHAPE;
   wq::LogprobsArgs a;
   a.logits = logits;
   a.f32 = dt == WQ_F32;
@@ -674,6 +673,7 @@ wq_status wq_token_logprobs(const void* logits, wq_dtype dt, int64_t T, int64_t 
   a.workspace = workspace;
   a.num_sms = d.num_sms;
   a.pdl = g_pdl.load();
+  if (workspace_bytes < wq::logprobs_workspace_needed(a)) return WQ_ERR_SHAPE;
   return cuda_status(wq::launch_token_logprobs(a, stream));
 }
 

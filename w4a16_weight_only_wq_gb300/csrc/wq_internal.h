@@ -156,6 +156,7 @@ struct LogprobsArgs {
   int pdl;
 };
 size_t logprobs_workspace_bytes(int64_t T, int64_t V, int k, int num_sms);
+size_t logprobs_workspace_needed(const LogprobsArgs& a);  // by this call
 cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t stream);
 
 }  // namespace wq

@@ -626,22 +626,35 @@ token_logprobs_kernel(const Params p) {
 // four per SM: bf16 30, 30, 39 us, fp32 28, 41, 35; bf16 cut to 64 registers for
 // four: 32), and at least two tiles a warp (joining two segments of one tile costs
 // 2.4 us, a second tile 1 us).
+int64_t most_segments(int64_t V) {
+  const int64_t n = V / (2 * kWarps * kTile);
+  return n < 1 ? 1 : n < kMaxSegments ? n : kMaxSegments;
+}
 int segments(int64_t T, int64_t V, int num_sms, bool f32) {
-  const int64_t want = (f32 ? 2 : 3) * static_cast<int64_t>(num_sms) / T;
-  const int64_t most = V / (2 * kWarps * kTile);
-  int64_t s = want < most ? want : most;
-  if (s < 1) s = 1;
-  return static_cast<int>(s < kMaxSegments ? s : kMaxSegments);
+  const int64_t want = (f32 ? 2 : 3) * static_cast<int64_t>(num_sms) / T, most = most_segments(V);
+  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
 }
 
-size_t counter_bytes(int64_t T) { return (static_cast<size_t>(T) * 4 + 255) / 256 * 256; }
+// The workspace: the rows' arrival counters, then a call's partials, then its
+// keys.  The counters' place does not depend on the call, so that what one call
+// leaves behind them is never another's counter: rows are split only while two
+// segments of each fit, so there are never more counters than this.
+size_t counter_bytes(int num_sms) { return (static_cast<size_t>(3 * num_sms / 2) * 4 + 255) / 256 * 256; }
+size_t segment_bytes(int k) { return sizeof(Partial) + 8 * static_cast<size_t>(k); }
 
 }  // namespace
 
+// For any call of up to T rows of up to V logits and up to k alternatives: where
+// rows are split, there are at most 3 SMs segments in all.
 size_t logprobs_workspace_bytes(int64_t T, int64_t V, int k, int num_sms) {
-  const size_t S = segments(T, V, num_sms, false);  // (fp32 logits take no more)
-  if (S == 1) return 256;
-  return counter_bytes(T) + static_cast<size_t>(T) * S * (sizeof(Partial) + 8 * static_cast<size_t>(k));
+  const int64_t row = most_segments(V), all = 3 * static_cast<int64_t>(num_sms);
+  const int64_t n = row == 1 ? 0 : T * row < all ? T * row : all;
+  return counter_bytes(num_sms) + static_cast<size_t>(n) * segment_bytes(k);
+}
+
+size_t logprobs_workspace_needed(const LogprobsArgs& a) {
+  const int S = segments(a.T, a.V, a.num_sms, a.f32);
+  return S == 1 ? 0 : counter_bytes(a.num_sms) + static_cast<size_t>(a.T) * S * segment_bytes(a.k);
 }
 
 cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t stream) {
@@ -671,8 +684,8 @@ cudaError_t launch_token_logprobs(const LogprobsArgs& a, cudaStream_t stream) {
     p.top_ids = a.top_ids == nullptr ? nullptr : a.top_ids + r * a.k;
     p.top_logprobs = a.top_logprobs == nullptr ? nullptr : a.top_logprobs + r * a.k;
     p.arrived = reinterpret_cast<uint32_t*>(ws) + r;
-    p.partials = reinterpret_cast<Partial*>(ws + counter_bytes(a.T)) + r * S;
-    p.keys = reinterpret_cast<uint64_t*>(ws + counter_bytes(a.T) + static_cast<size_t>(a.T) * S * sizeof(Partial)) + r * S * a.k;
+    p.partials = reinterpret_cast<Partial*>(ws + counter_bytes(a.num_sms)) + r * S;
+    p.keys = reinterpret_cast<uint64_t*>(ws + counter_bytes(a.num_sms) + static_cast<size_t>(a.T) * S * sizeof(Partial)) + r * S * a.k;
     cfg.gridDim = dim3(static_cast<unsigned>(S), static_cast<unsigned>(n));
     cudaError_t e;
     if (a.f32)
