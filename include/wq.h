@@ -338,8 +338,9 @@ WQ_API int wq_debug_kv4_sequence(int64_t cu0, int64_t cu1, int64_t kv_len, int64
  * value rounded once to fp32, x; then s = bf16(max|x| / 7) over its group (1
  * where that is 0) and q = clamp(rint(x / s), -8, 7), divisions in IEEE
  * fp32, ties to even.  A group with a NaN or an infinity gets the scale NaN
- * and codes 0, so that whatever reads it sees NaN.  A token whose page or
- * position lies outside is not written (its Q_out row is zeros).
+ * and codes 0, so that whatever reads it sees NaN.  A token whose slot, page or
+ * position lies outside is not written (its Q_out row is zeros); its slot
+ * follows from cu_q and kv_len as they are, so no other token's is written.
  * No two tokens of a call may share a slot.  Errors: WQ_ERR_NULL,
  * WQ_ERR_SHAPE, WQ_ERR_ALIGN, WQ_ERR_UNSUPPORTED (device), WQ_ERR_CUDA.
  * Stream-ordered; allocates nothing.

@@ -131,8 +131,10 @@ __device__ __forceinline__ void find_slots(const Kv4Params& p, int64_t tok0, int
     s.in_page = 0;
     const int b = seqs[threadIdx.x];
     if (b >= 0) {
+      // a token's slot follows from the entries as they are: clamped ones would
+      // move it onto a slot that is another token's
       const Kv4Seq q = kv4_load_sequence(p, b);
-      s.pos = q.len - q.n + (tok0 + threadIdx.x - q.first);
+      s.pos = __ldg(p.kv_len + b) - (__ldg(p.cu_q + b + 1) - (tok0 + threadIdx.x));
       s.block = -1;
       if (s.pos >= 0 && s.pos < q.len) {
         const int64_t page = __ldg(p.page_table + b * p.max_pages + (s.pos >> p.lay.page_shift));
