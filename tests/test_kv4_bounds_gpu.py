@@ -57,3 +57,20 @@ def test_append_and_read_touch_the_tokens_own_slots_only(wq, cu, kv, slots):  # 
     torch.cuda.synchronize()
     assert wq.wq_last_device_error() == wq.WQ_ERR_DEVICE_BOUNDS
     wq.wq_clear_device_error()
+
+
+@pytest.mark.parametrize("cu,kv", [
+    ([0, 1, 1], [20, -1]),          # sequences without new tokens: a length below zero,
+    ([0, 1, 1], [20, 65]),          # one past the table's 64 slots,
+    ([0, 1, 0], [20, 30]),          # entries that descend
+])
+def test_sequences_without_new_tokens_are_checked_too(wq, cu, kv):  # noqa: F811
+    st = Step(wq, [1, 0], [64, 64], D=64, group=32, page=16, Hkv=1, seed=51)
+    batch = wq.kv4_batch(st.batch.page_table, _i32(cu), _i32(kv), 1, max_q=1)
+    x = torch.ones((1, 1, 64), dtype=torch.bfloat16, device=dev())
+    for call in (lambda: wq.kv4_append(st.cache, batch, x, x), lambda: wq.kv4_read(st.cache, batch),
+                 lambda: wq.kv4_attention(x, st.cache, batch)):
+        call()
+        torch.cuda.synchronize()
+        assert wq.wq_last_device_error() == wq.WQ_ERR_DEVICE_BOUNDS
+        wq.wq_clear_device_error()

@@ -120,6 +120,7 @@ __device__ __forceinline__ void find_slots(const Kv4Params& p, int64_t tok0, int
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kThreads) {
     const int64_t c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
+    if (blockIdx.x == 0) kv4_load_sequence(p, b);  // records what does not fit, also of a sequence without new tokens
     for (int i = 0; i < n; ++i)
       if (c0 <= tok0 + i && tok0 + i < c1) atomicMax(seqs + i, b);
   }
