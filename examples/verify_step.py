@@ -5,8 +5,9 @@ itself, but checks blocks of drafted tokens against a 4-bit key/value cache.
 
 A layer is: projection to queries, keys and values (``gemm_w4a16``), rotation and the cache's new rows
 (``kv4_append``), attention over the cache (``kv4_attention``), output projection, MLP (``mlp``).  The logits of the
-block's rows (``gemm_w8a16``) go to ``token_logprobs``: a drafted token whose rank is 0 is what greedy decoding would
-have chosen, so the longest prefix of such tokens is kept.  Lengths, page tables and tokens are device tensors, so one
+block's rows (``gemm_w8a16``) go to ``token_logprobs``: a drafted token that is the first of the row's top ids is what
+greedy decoding would have chosen (a rank of 0 is not enough: bf16 logits often tie, and greedy decoding takes the lowest
+id), so the longest prefix of such tokens is kept.  Lengths, page tables and tokens are device tensors, so one
 captured graph serves every step; a sequence's rejected tokens are simply overwritten by the next block.
 """
 import argparse
@@ -69,8 +70,8 @@ class Verifier:
         alternatives: (kept [seqs], logprob [seqs, block - 1], top ids [T, k])."""
         logits = self.logits(tokens, batch)
         drafted = tokens.view(-1, block).roll(-1, 1).flatten()  # (a block's last row has no drafted successor)
-        logprob, _, rank, top, _ = wq.token_logprobs(logits, drafted, k)
-        right = (rank.view(-1, block)[:, :-1] == 0).int()
+        logprob, _, _, top, _ = wq.token_logprobs(logits, drafted, k)
+        right = (top[:, 0] == drafted).view(-1, block)[:, :-1].int()
         return 1 + right.cumprod(1).sum(1), logprob.view(-1, block)[:, :-1], top
 
 

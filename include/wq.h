@@ -405,7 +405,7 @@ WQ_API size_t wq_logprobs_workspace_bytes(int64_t T, int64_t V, int k);
  * What verification reads off the target's logits, in one pass over them:
  * with y_j = t x_j of row x (t the row's inverse temperature, 1 without),
  *     logprob = y_tok - log sum_j exp(y_j)      entropy = -sum_j p_j log p_j
- *     rank    = number of ids with x_j > x_tok
+ *     rank    = number of ids with x_j > x_tok (ids that tie share it)
  *     top_ids, top_logprobs = the k largest x_j, largest first, equal values
  *               by the lowest id, and their log probabilities
  *   logits    [T][V] fp32 or bf16 (dt), rows row_stride elements apart, any

@@ -620,7 +620,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, k: int = 0,
                    inv_temperature: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Per row of logits [T, V] (fp32 or bf16, rows any distance apart) and its token (int64 [T]): returns (log
     probability [T], entropy [T], rank [T] int32, top ids [T, k] int32, top log probabilities [T, k]) of the softmax
-    of inv_temperature * logits; equal logits rank by the lowest id."""
+    of inv_temperature * logits.  The rank is the number of larger logits, so tokens that tie share it; the top ids put
+    the lowest id of equal logits first."""
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits must be [T, V], float32 or bfloat16")
     T, V = logits.shape
