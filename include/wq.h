@@ -294,8 +294,9 @@ typedef struct {
   const int32_t* cu_q;       /* [num_seqs + 1], cu_q[0] = 0 */
   const int32_t* kv_len;     /* [num_seqs] */
   int64_t num_seqs, num_tokens, max_pages;
-  int64_t max_q;             /* most new tokens of one sequence; 0: not known.  A hint that
-                                picks the kernel (they round differently); any value is right */
+  int64_t max_q;             /* most new tokens of one sequence; 0: not known, taken as num_tokens
+                                - num_seqs + 1 (exact where all have one).  A hint that picks the
+                                kernel (they round differently); any value is right, a wrong one slow */
 } wq_kv4_batch;
 
 /* bf16 rows [num_tokens][heads][D] anywhere in device memory: strides in

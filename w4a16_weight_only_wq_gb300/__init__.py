@@ -516,8 +516,9 @@ class Kv4Batch:
 def kv4_batch(page_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, tokens: int,
               max_q: int = 0) -> Kv4Batch:
     """page_table int32 [B, pages], cu_q int32 [B + 1] (prefix sums of the new tokens), kv_len int32 [B] (cached
-    tokens, the new ones included), ``tokens`` new tokens in all, at most ``max_q`` of one sequence (0: not known).
-    Every layer of a step uses the same batch."""
+    tokens, the new ones included), ``tokens`` new tokens in all, at most ``max_q`` of one sequence.  ``max_q`` picks the
+    attention's kernel; 0 (not known) is guessed from the number of tokens and sequences, rightly for single tokens, but
+    blocks of several sequences run up to a fifth slower than with it.  Every layer of a step uses the same batch."""
     for name, t, shape in (("page_table", page_table, None), ("cu_q", cu_q, (page_table.shape[0] + 1,)),
                            ("kv_len", kv_len, (page_table.shape[0],))):
         if t.dtype != torch.int32 or not t.is_contiguous():

@@ -353,7 +353,13 @@ wq_status kv4_args(const wq_kv4_cache* c, const wq_kv4_batch* b, wq::Kv4Args* a)
   a->max_pages = b->max_pages;
   a->B = b->num_seqs;
   a->T = b->num_tokens;
-  a->max_q = b->max_q;
+  // Not known: as many as one sequence has if every other has one token, which is
+  // what all have in a decoding step.  (With all tokens taken as one sequence's, 64
+  // single tokens of four grouped heads of 128 went to the many-row kernel: 289 us
+  // over 4096 keys each instead of 70, 107 over 1000 instead of 27.  For 8 blocks of
+  // 16 the guess is high: 152 us over 16384 keys where the hint gives 128.)
+  const int64_t guess = b->num_tokens > b->num_seqs ? b->num_tokens - b->num_seqs + 1 : 1;
+  a->max_q = b->max_q == 0 ? guess : b->max_q < b->num_tokens ? b->max_q : b->num_tokens;
   a->page_size = c->page_size;
   a->Hkv = c->Hkv;
   a->D = c->D;

@@ -8,7 +8,7 @@ cudaError_t launch_kv4_split_d128(const Kv4Args& a, const Kv4AttentionArgs& x, c
   const int G = a.D / a.group;
   // A tile of 8 rows where no sequence has more, else 16: one tile of 16
   // reads the codes once where two of 8 read them twice.
-  const bool small = (a.max_q > 0 ? a.max_q : a.T) * (x.Hq / a.Hkv) <= 8;
+  const bool small = a.max_q * (x.Hq / a.Hkv) <= 8;
   if (G == 1) return small ? launch_variant<128, 1, 1>(a, x, stream) : launch_variant<128, 1, 2>(a, x, stream);
   if (G == 2) return small ? launch_variant<128, 2, 1>(a, x, stream) : launch_variant<128, 2, 2>(a, x, stream);
   if (G == 4) return small ? launch_variant<128, 4, 1>(a, x, stream) : launch_variant<128, 4, 2>(a, x, stream);
@@ -31,7 +31,7 @@ cudaError_t launch_kv4_attention(const Kv4Args& a, const Kv4AttentionArgs& x, cu
   // 46 / 55; one of 16384: 46 / 63 / 98 against 46 / 60 / 89; 16 rows 117 against 20 rows
   // 124.  (Of a few short sequences the few-row kernel does better up to 64
   // rows, by 10 us; how long they are is not known here.)
-  const int64_t rows = (a.max_q > 0 ? a.max_q : a.T) * (x.Hq / a.Hkv);  // of one head of a sequence, at most
+  const int64_t rows = a.max_q * (x.Hq / a.Hkv);  // of one head of a sequence, at most
   if (a.D != 256 && rows > 16)
     return a.D == 64 ? launch_kv4_tile_d64(a, x, stream) : launch_kv4_tile_d128(a, x, stream);
   if (a.D == 64) return launch_kv4_split_d64(a, x, stream);

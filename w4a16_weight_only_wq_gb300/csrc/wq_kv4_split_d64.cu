@@ -8,7 +8,7 @@ cudaError_t launch_kv4_split_d64(const Kv4Args& a, const Kv4AttentionArgs& x, cu
   const int G = a.D / a.group;
   // A tile of 8 rows where no sequence has more, else 16: one tile of 16
   // reads the codes once where two of 8 read them twice.
-  const bool small = (a.max_q > 0 ? a.max_q : a.T) * (x.Hq / a.Hkv) <= 8;
+  const bool small = a.max_q * (x.Hq / a.Hkv) <= 8;
   if (G == 1) return small ? launch_variant<64, 1, 1>(a, x, stream) : launch_variant<64, 1, 2>(a, x, stream);
   if (G == 2) return small ? launch_variant<64, 2, 1>(a, x, stream) : launch_variant<64, 2, 2>(a, x, stream);
   return cudaErrorNotSupported;
