@@ -385,7 +385,7 @@ WQ_API size_t wq_kv4_workspace_bytes(int64_t Hq, int Hkv, int D);
  * zeros.  Slots at or past kv_len are never used, whatever they hold.
  *   Q, O      rows of Hq heads, Hq a multiple of Hkv, Hq / Hkv <= 64;
  *             finite values; O must not overlap Q
- *   scale     positive and finite
+ *   scale     positive, up to 2e38
  *   workspace wq_kv4_workspace_bytes(Hq, Hkv, D) bytes, 16-byte aligned
  * Results do not depend on timing.  Errors: WQ_ERR_NULL, WQ_ERR_SHAPE,
  * WQ_ERR_ALIGN, WQ_ERR_UNSUPPORTED (device), WQ_ERR_CUDA.  Stream-ordered;

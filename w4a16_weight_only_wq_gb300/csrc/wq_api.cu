@@ -618,7 +618,7 @@ wq_status wq_kv4_attention(const wq_kv4_cache* cache, const wq_kv4_batch* batch,
   wq_status st = check_kv4(cache, batch);
   if (st != WQ_OK) return st;
   if (Hq < cache->Hkv || Hq % cache->Hkv != 0 || Hq / cache->Hkv > 64 || window < 0) return WQ_ERR_SHAPE;
-  if (!(scale > 0.f) || !(scale <= 3.0e38f)) return WQ_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale <= 2.0e38f)) return WQ_ERR_SHAPE;  // (the kernels take scale * log2 e)
   if (batch->num_tokens == 0 || batch->num_seqs == 0) return WQ_OK;
   if ((st = check_rows(Q, Hq, batch)) != WQ_OK || (st = check_rows(O, Hq, batch)) != WQ_OK) return st;
   if (!workspace) return WQ_ERR_NULL;
