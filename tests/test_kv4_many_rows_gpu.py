@@ -102,3 +102,24 @@ def test_a_wait_that_runs_out_leaves_the_workspace_fit(wq):  # noqa: F811
     assert not counters.any()
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(want, both()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("largest", [2.0 ** -7, 1.0, 2.0 ** 14, 2.0 ** 15])
+@pytest.mark.parametrize("tokens,kv", [(20, 150), (40, 400)])
+def test_queries_with_one_large_dimension(wq, D, largest, tokens, kv):  # noqa: F811
+    """A dimension that no key has, 2^8 of the others' size, and scores from those others alone: they count with all
+    their bits whatever the size of the largest (a bf16 query is exact, so only the products' sums round)."""
+    st = Step(wq, [tokens], [kv], D=D, group=D, page=32, Hkv=1, seed=70)
+    for p in range(st.pool.shape[0]):  # key codes of dimension 0: none
+        n = st.page * D // 2
+        words = st.pool[p, 0][:n].view("<u4").reshape(st.page, D // 8)
+        w, nib = kv4_ref.key_place(D, 0)
+        words[:, w] = (words[:, w] & ~np.uint32(15 << (4 * nib))) | np.uint32(8 << (4 * nib))
+    st.upload(wq)
+    Q = np.random.default_rng(71).normal(size=(tokens, 4, D)) * largest * 2.0 ** -8
+    Q[:, :, 0] = largest
+    bits = kv4_ref.bf16(Q)
+    scale = 30 / (largest * 2.0 ** -8 * D ** 0.5 * 1.5)  # scores of some tens
+    O = wq.kv4_attention(bf16_to_dev(bits).view(tokens, 4, D), st.cache, st.batch, scale=scale)
+    st.check(bits, O, 4, float(np.float32(scale)), many_rows=True)

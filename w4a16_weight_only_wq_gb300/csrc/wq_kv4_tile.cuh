@@ -342,8 +342,8 @@ static __device__ __noinline__ void shrink(uint32_t ts, int wcols, uint32_t to, 
 // usual block, and it reads next to nothing from shared memory: 64 loads of
 // factors a row and block made it 1.7 times as slow under the other stream's
 // scores, which read their operands from there at its full rate.
-// Otherwise only the columns lo .. hi count, each key has its own factors
-// (kfac, vfac), and scores are multiplied by row_scale.
+// Otherwise only the columns lo .. hi count, and each key has its own factors
+// (kfac, vfac).  Scores are multiplied by row_scale.
 //
 // A weight that has left fp16 (or, where value factors are tiny, fp32's
 // middle) moves the row's reference up and shrinks what the row has so far.
@@ -375,7 +375,7 @@ __device__ __forceinline__ void weigh_block(uint32_t ts, uint32_t to, const floa
         tmem_ld_wait_regs(raw);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float k = u ? gb.x : ga.x, nr = (u ? gb.y : ga.y) - ref;
+          const float k = (u ? gb.x : ga.x) * row_scale, nr = (u ? gb.y : ga.y) - ref;
           const uint64_t k2 = pair(k, k), nr2 = pair(nr, nr);
           uint64_t sums[2] = {0, 0};
 #pragma unroll
@@ -735,10 +735,11 @@ kv4_tile_kernel(const TileParams tp) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) top = max(top, max(e[j] & 0x7FFFu, (e[j] >> 16) & 0x7FFFu));
         }
-        // fp16 holds a bf16 query whose largest value is moderate; another one
-        // is normalised by a power of two
+        // fp16 holds the row normalised by a power of two, so that its largest
+        // value is 2^12 or above: all bits of those down to 2^-26 of it.  (As they
+        // are, values below 2^-14 would lose bits beside one of 2^-8.)
         const float big = __uint_as_float(top << 16);
-        row_scale = big == 0.f || (big >= 0x1p-8f && big < 0x1p15f) ? 1.f : pow2_floor(fmaxf(big, 1e-30f)) * 0x1p-12f;
+        row_scale = pow2_floor(fmaxf(big, 1e-30f)) * 0x1p-12f;
         const float inv = 1.0f / row_scale;
         if (NT == 2 || stream == 0) {
           const uint32_t dst = sb + S::kOffQ + (NT == 2 ? stream * S::kQ : 0);
@@ -762,7 +763,6 @@ kv4_tile_kernel(const TileParams tp) {
       const bool alone = it.rows <= 128;
       auto block_of = [&](int i) { return NT == 2 ? i : 2 * i + stream; };  // of the item's n
       if (issuer && ok && my > 0) issue_scores(n_block + block_of(0));
-      const bool plain = __all_sync(0xffffffffu, row_scale == 1.f);
       const bool busy = __any_sync(0xffffffffu, live);  // else nobody reads what the products make of these rows
       // positions of the live rows of this warp's tile half, for the mask
       const int pf = NT == 2 && stream == 1 ? p0 + static_cast<int>((it.row0 + 128) / p.gq) : it.pos_first;
@@ -789,8 +789,8 @@ kv4_tile_kernel(const TileParams tp) {
           const int4* even = reinterpret_cast<const int4*>(smem + S::kOffEven) + ((n_block + blk) % kFacRing) * 2;
           const int4 ea = even[0], eb = even[1];
           const Granule* gran = reinterpret_cast<const Granule*>(smem + S::kOffGran) + ((n_block + blk) % kFacRing) * 8;
-          if (interior && plain && (ea.x & ea.y & ea.z & ea.w & eb.x & eb.y & eb.z & eb.w))
-            weigh_block<D, true>(ts, to, kfac, vfac, gran, 1.f, lo, hi, i > 0, ref, L);
+          if (interior && (ea.x & ea.y & ea.z & ea.w & eb.x & eb.y & eb.z & eb.w))
+            weigh_block<D, true>(ts, to, kfac, vfac, gran, row_scale, lo, hi, i > 0, ref, L);
           else
             weigh_block<D, false>(ts, to, kfac, vfac, gran, row_scale, lo, hi, i > 0, ref, L);
           tmem_st_wait();
