@@ -377,9 +377,9 @@ WQ_API size_t wq_kv4_workspace_bytes(int64_t Hq, int Hkv, int D);
  * with fp32 scores, softmax statistics and sums; a weight times its value's
  * scale (or the power of two below it) is rounded to fp16 (11 significant
  * bits, for products down to 2^-20 of the row's largest), O once to bf16.
- * Where a sequence has more than 16 rows (tokens times Hq / Hkv; D 64 and 128)
- * the scales of one key or value are held relative to the largest of them, in
- * fp16: those below 2^-17 of it lose bits.  Query head h reads key/value head
+ * Where a sequence has more than 16 rows (tokens times Hq / Hkv; 64 where D is
+ * 64; D 256 has no such kernel) the scales of one key or value are held relative
+ * to the largest of them, in fp16: those below 2^-17 of it lose bits.  Query head h reads key/value head
  * h / (Hq / Hkv).  A value scale of NaN makes the rows that see it NaN, in its
  * group at least.  A query that sees no key (kv_len < q_len) gives
  * zeros.  Slots at or past kv_len are never used, whatever they hold.
@@ -447,7 +447,7 @@ WQ_API const char* wq_last_cuda_error(void);
    wq_debug_force_timeout(mode): 0 off; 1 every CTA of the next GEMMs first
    waits on a barrier nothing completes -- the wait runs out, is reported,
    and the GEMM then runs normally; 2 the data waits look for a phase that
-   never completes, so the GEMM (or wq_kv4_attention of more than 16 rows)
+   never completes, so the GEMM (or wq_kv4_attention of many rows)
    gives up, lets its copies and products finish and reports (its output is
    then undefined).  Both report WQ_ERR_DEVICE_TIMEOUT through
    wq_last_device_error() without any fault. */

@@ -1,5 +1,5 @@
-"""The many-row attention over the 4-bit cache (more than 16 rows of a head and
-sequence, heads of 64 and 128) where its own paths can go wrong."""
+"""The many-row attention over the 4-bit cache (more than 16 rows of a head of 128
+and sequence, or 64 of a head of 64) where its own paths can go wrong."""
 import numpy as np
 import pytest
 import torch
@@ -33,7 +33,7 @@ def _scales(st, value, b, h, keys, scale):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("tokens", [10, 60])           # 40 rows (one tile), 240 (two)
+@pytest.mark.parametrize("tokens", [10, 25, 60])       # 40 and 100 rows (one tile), 240 (two)
 @pytest.mark.parametrize("per_key", [False, True])     # keys that share their factors, and keys that do not
 @pytest.mark.parametrize("column", [5, 40, 70, 100, 127])
 def test_a_larger_score_late_in_a_block(wq, D, tokens, per_key, column):  # noqa: F811

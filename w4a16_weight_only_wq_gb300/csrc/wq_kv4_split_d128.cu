@@ -23,17 +23,21 @@ size_t kv4_workspace_bytes(int D, int num_sms) {
 }
 
 cudaError_t launch_kv4_attention(const Kv4Args& a, const Kv4AttentionArgs& x, cudaStream_t stream) {
-  // More than 16 rows of a head and sequence go to the many-row kernel, which reads
-  // the codes once for up to 256 rows where this one reads them once for 16.  us at
-  // 32 / 64 / 128 rows (32 query, 8 key/value heads of 128), few-row kernel against
-  // many-row: 8 sequences of 16384: 223 / 424 / 826 against 122 / 126 / 140; 32 of
-  // 4096: 217 / 415 / 834 against 138 / 144 / 161; 8 of 1024: 31 / 46 / 65 against 40 /
-  // 46 / 55; one of 16384: 46 / 63 / 98 against 46 / 60 / 89; 16 rows 117 against 20 rows
-  // 124.  (Of a few short sequences the few-row kernel does better up to 64
-  // rows, by 10 us; how long they are is not known here.)
+  // More than 16 rows of a head and sequence (64, for heads of 64) go to the many-row
+  // kernel, which reads the codes once for up to 256 rows where this one reads them
+  // once for 16.  Heads of 128 (32 query and 8 key/value heads), us at 32 / 64 / 128
+  // rows, few-row kernel against many-row: 8 sequences of 16384: 223 / 424 / 826
+  // against 122 / 126 / 140; 32 of 4096: 217 / 415 / 834 against 138 / 144 / 161; 8 of
+  // 1024: 31 / 46 / 65 against 40 / 46 / 55; one of 16384: 46 / 63 / 98 against 46 / 60
+  // / 89; 16 rows 119 against 20 rows 125.  (Of a few short sequences the few-row
+  // kernel does better up to 64 rows, by 10 us; how long they are is not known here.)
+  // Heads of 64, at 32 / 48 / 64 rows: 8 of 16384: 66 / 90 / 113 against 108 / 108 /
+  // 108; 32 of 4096: 68 / 93 / 120 against 118 / 118 / 119; 8 of 1024: 21 / 23 / 28
+  // against 34 / 34 / 35; one of 16384: 27 / 24 / 31 against 42 / 43 / 43: the many-row
+  // kernel's chain for a block hardly shrinks with the dimensions.
   const int64_t rows = a.max_q * (x.Hq / a.Hkv);  // of one head of a sequence, at most
-  if (a.D != 256 && rows > 16)
-    return a.D == 64 ? launch_kv4_tile_d64(a, x, stream) : launch_kv4_tile_d128(a, x, stream);
+  if (a.D == 64 && rows > 64) return launch_kv4_tile_d64(a, x, stream);
+  if (a.D == 128 && rows > 16) return launch_kv4_tile_d128(a, x, stream);
   if (a.D == 64) return launch_kv4_split_d64(a, x, stream);
   if (a.D == 128) return launch_kv4_split_d128(a, x, stream);
   return launch_kv4_split_d256(a, x, stream);
