@@ -324,6 +324,10 @@ WQ_API int64_t wq_kv4_locate(const wq_kv4_cache* cache, int64_t page, int head, 
 WQ_API int wq_debug_kv4_sequence(int64_t cu0, int64_t cu1, int64_t kv_len, int64_t num_tokens,
                                  int64_t capacity, int64_t* out);
 
+/* out[i] = in[i] / 7 for the scale of a group whose largest |x| is in[i], from
+   2^-100 to 2^100 (test hook, as above; host arrays). */
+WQ_API void wq_debug_kv4_seventh(const float* in, float* out, int64_t n);
+
 /*
  * Append the new tokens: rotate queries and keys by position, write the
  * rotated queries to Q_out, round keys and values to 4 bits and write them

@@ -46,7 +46,8 @@ EXPORTED = (
     "wq_clear_device_error", "wq_status_string", "wq_debug_set_wait_limit_ns",
     "wq_debug_force_timeout", "wq_gemm_regime", "wq_debug_set_split",
     "wq_set_programmatic_launch", "wq_last_cuda_error", "wq_debug_force_regime",
-    "wq_kv4_pool_bytes", "wq_kv4_locate", "wq_debug_kv4_sequence", "wq_kv4_append", "wq_kv4_read",
+    "wq_kv4_pool_bytes", "wq_kv4_locate", "wq_debug_kv4_sequence", "wq_debug_kv4_seventh",
+    "wq_kv4_append", "wq_kv4_read",
     "wq_kv4_workspace_bytes", "wq_kv4_attention", "wq_logprobs_workspace_bytes", "wq_token_logprobs",
 )
 
@@ -109,6 +110,7 @@ def _load() -> ctypes.CDLL:
         "wq_kv4_pool_bytes": ([I64, I, I, I, I], ctypes.c_size_t),
         "wq_kv4_locate": ([C, I64, I, I, I, I, P, P], I64),
         "wq_debug_kv4_sequence": ([I64, I64, I64, I64, I64, P], I),
+        "wq_debug_kv4_seventh": ([P, P, I64], None),
         "wq_kv4_append": ([C, B, R, R, I64, R, R, P, I64, I, I, P, P], I),
         "wq_kv4_read": ([C, B, R, R, P], I),
         "wq_kv4_workspace_bytes": ([I64, I, I], ctypes.c_size_t),
@@ -397,6 +399,11 @@ def wq_debug_kv4_sequence(cu0, cu1, kv_len, num_tokens, capacity):
     out = (ctypes.c_int64 * 3)()
     bad = _lib.wq_debug_kv4_sequence(cu0, cu1, kv_len, num_tokens, capacity, out)
     return (int(bad), *out)
+
+
+def wq_debug_kv4_seventh(values, out, n) -> None:
+    """Host addresses of n floats each."""
+    _lib.wq_debug_kv4_seventh(values, out, n)
 
 
 def wq_kv4_append(cache, batch, Q, Q_out, Hq, K, V, rope, max_pos, rot_dim, interleaved, positions,

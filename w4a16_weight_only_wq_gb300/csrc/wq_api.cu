@@ -562,6 +562,10 @@ int wq_debug_kv4_sequence(int64_t cu0, int64_t cu1, int64_t kv_len, int64_t num_
   return s.bad ? 1 : 0;
 }
 
+void wq_debug_kv4_seventh(const float* in, float* out, int64_t n) {
+  for (int64_t i = 0; i < n; ++i) out[i] = wq::kv4_seventh(in[i]);
+}
+
 wq_status wq_kv4_append(const wq_kv4_cache* cache, const wq_kv4_batch* batch, const wq_rows* Q, const wq_rows* Q_out,
                         int64_t Hq, const wq_rows* K, const wq_rows* V, const float* rope, int64_t max_pos,
                         int rot_dim, int interleaved, const int32_t* positions, cudaStream_t stream) {

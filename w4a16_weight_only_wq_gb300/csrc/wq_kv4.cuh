@@ -4,6 +4,7 @@
 // include/wq.h.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -52,6 +53,18 @@ __host__ __device__ inline void kv4_key_nibble(int D, int dim, int* word, int* n
 __host__ __device__ inline void kv4_value_nibble(int D, int dim, int* word, int* nibble) {
   *word = (dim & 7) * (D >> 6) + (dim >> 6);
   *nibble = (dim >> 3) & 7;
+}
+
+// t / 7 without a division: a product with 1/7 and one correction by the
+// remainder, which is exact.  For t from 2^-100 to 2^100 it is the quotient as
+// IEEE division rounds it (the tests compare every mantissa).
+__host__ __device__ inline float kv4_seventh(float t) {
+#ifdef __CUDA_ARCH__
+  const float q = __fmul_rn(t, 1.f / 7.f);
+#else
+  const float q = t * (1.f / 7.f);
+#endif
+  return fmaf(fmaf(-q, 7.f, t), 1.f / 7.f, q);
 }
 
 // One sequence's entries, clamped to what the call's buffers hold.

@@ -83,14 +83,12 @@ __device__ __forceinline__ uint32_t key_word(uint32_t w) {
 // Eight values' scale, and their codes as nibbles in order, without a
 // division; false (for the whole warp) where a value
 // lies so near a border between two codes, or the group so far from 1, that
-// only the division decides.  max / 7 by a product with 1/7 and one correction
-// is the correctly rounded quotient (checked for every mantissa); x times a
-// reciprocal is off by 2^-21 of at most 7.03, so a code is sure unless the
-// product comes within 1e-5 of a half.
+// only the division decides.  max / 7 is the correctly rounded quotient
+// (kv4_seventh); x times a reciprocal is off by 2^-21 of at most 7.03, so a code is
+// sure unless the product comes within 1e-5 of a half.
 __device__ __forceinline__ bool grid_fast(const float (&x)[8], uint32_t top, float& scale, uint32_t& word) {
   const float t = __uint_as_float(top);
-  const float q0 = __fmul_rn(t, 1.f / 7.f), q1 = __fmaf_rn(__fmaf_rn(-q0, 7.f, t), 1.f / 7.f, q0);
-  scale = t == 0.f ? 1.f : __bfloat162float(__float2bfloat16_rn(q1));
+  scale = t == 0.f ? 1.f : __bfloat162float(__float2bfloat16_rn(kv4_seventh(t)));
   bool unsure = t != 0.f && !(t > 0x1p-100f && t < 0x1p100f);
   const float inv = __fdividef(1.f, scale);
   constexpr float kRound = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
