@@ -6,7 +6,7 @@ import torch
 
 from tests import kv4_ref
 from tests.gpu_util import bf16_to_dev, dev
-from tests.test_kv4_gpu import Step, _no_error, wq  # noqa: F401  (fixtures)
+from tests.test_kv4_gpu import Step, _attend, _i32, _no_error, _queries, wq  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,128 @@ def test_queries_with_one_large_dimension(wq, D, largest, tokens, kv):  # noqa: 
     scale = 30 / (largest * 2.0 ** -8 * D ** 0.5 * 1.5)  # scores of some tens
     O = wq.kv4_attention(bf16_to_dev(bits).view(tokens, 4, D), st.cache, st.batch, scale=scale)
     st.check(bits, O, 4, float(np.float32(scale)), many_rows=True)
+
+
+MANY = [(64, 96), (128, 20)]  # heads of, and tokens with four grouped heads that take this kernel
+
+
+@pytest.mark.parametrize("D,n", MANY)
+@pytest.mark.parametrize("at", [0, 3, -1])   # the first page, one in the middle of a block, the last
+def test_pages_outside_are_reported_and_not_followed(wq, D, n, at):  # noqa: F811
+    """The other sequence's rows are what they are without the bad page."""
+    st = Step(wq, [n, n], [300, 400], D=D, group=D // 2, page=16, Hkv=1, seed=80)
+    bits, O = _attend(wq, st, Hq=4)
+    last = -(-st.kv[0] // 16) - 1
+    for bad in (-1, st.pool.shape[0], 2 ** 31 - 1, -2 ** 31):
+        st.table[0, at if at >= 0 else last] = bad
+        st.upload(wq)
+        before = st.cache.pool.clone()
+        _, O2 = _attend(wq, st, Hq=4)
+        torch.cuda.synchronize()
+        assert wq.wq_last_device_error() == wq.WQ_ERR_DEVICE_BOUNDS
+        wq.wq_clear_device_error()
+        assert torch.equal(O[n:], O2[n:]) and torch.equal(before, st.cache.pool)
+
+
+@pytest.mark.parametrize("D,n", MANY)
+def test_lengths_outside_are_clamped_and_reported(wq, D, n):  # noqa: F811
+    st = Step(wq, [n, n], [300, 400], D=D, group=D, page=16, Hkv=1, seed=81)
+    bits, O = _attend(wq, st, Hq=4)
+    Q = bf16_to_dev(bits).view(2 * n, 4, D)
+    for cu, kv, untouched in (([0, n, 5 * n], [300, 400], 0), ([0, n, 2 * n], [300, 2 ** 31 - 1], 0),
+                              ([0, n, 2 * n], [-5, 400], 1), ([-9, n, 2 * n], [300, 400], 1),
+                              ([0, n, 2 * n], [300, 400 + 16 * 16], 0)):
+        batch = wq.kv4_batch(st.batch.page_table, _i32(cu), _i32(kv), 2 * n, max_q=n)
+        O2 = wq.kv4_attention(Q, st.cache, batch)
+        torch.cuda.synchronize()
+        assert wq.wq_last_device_error() == wq.WQ_ERR_DEVICE_BOUNDS
+        wq.wq_clear_device_error()
+        rows = slice(untouched * n, untouched * n + n)
+        assert torch.equal(O[rows], O2[rows])
+
+
+@pytest.mark.parametrize("D,n", MANY)
+def test_offsets_past_32_bits(wq, D, n):  # noqa: F811
+    """A pool of over 4 GiB whose last pages hold the sequence."""
+    block = kv4_ref.block_bytes(256, D, D)
+    P = (1 << 32) // (2 * block) + 40
+    st = Step(wq, [n], [600], D=D, group=D, page=256, Hkv=2, seed=82, spare=0)
+    bits, want = _attend(wq, st, Hq=8)
+    pool = torch.zeros((P, 2, block), dtype=torch.uint8, device=dev())
+    pool[-3:] = st.cache.pool[torch.tensor(st.table[0], device=dev())]
+    st.cache = wq.kv4_cache(P, 2, D, 256, D, pool=pool)
+    st.batch = wq.kv4_batch(_i32([[P - 3, P - 2, P - 1]]), _i32([0, n]), _i32([600]), n, max_q=n)
+    _, O = _attend(wq, st, Hq=8)
+    assert torch.equal(O, want)
+    st.check(bits, O, 8, D ** -0.5, many_rows=True)
+
+
+@pytest.mark.parametrize("D,n", MANY)
+def test_strided_rows_and_tokens_of_no_sequence(wq, D, n):  # noqa: F811
+    st = Step(wq, [n, n - 3], [150, 160], D=D, group=D, page=16, Hkv=2, seed=83)
+    T = st.T + 4
+    bits = _queries(st.rng, T, 8, D)
+    wide = torch.full((T, 11, 2 * D), 3.0, dtype=torch.bfloat16, device=dev())
+    wide[:, 2:10, D:] = bf16_to_dev(bits).view(T, 8, D)
+    out = torch.full((8, T, D), 7.0, dtype=torch.bfloat16, device=dev())
+    batch = wq.kv4_batch(st.batch.page_table, st.batch.cu_q, st.batch.kv_len, T, max_q=n)
+    O = wq.kv4_attention(wide[:, 2:10, D:], st.cache, batch, O=out.transpose(0, 1))
+    st.check(bits[:st.T], O[:st.T].contiguous(), 8, D ** -0.5, many_rows=True)
+    assert (O[st.T:] == 7).all()
+
+
+@pytest.mark.parametrize("D,n", MANY)
+def test_side_stream_and_graph_with_growing_lengths(wq, D, n):  # noqa: F811
+    """Blocks of the same size after ever longer sequences, from one captured graph; the lengths pass a page and a
+    block of 128 keys."""
+    st = Step(wq, [n, n], [n + 7, 230], D=D, group=D, page=16, Hkv=2, seed=84, spare=40)
+    free = sorted(set(range(st.pool.shape[0])) - {int(x) for x in st.table.flatten() if x >= 0})
+    table = np.full((2, 40), -1)
+    for b in range(2):
+        used = -(-st.kv[b] // 16)
+        table[b, :used] = st.table[b, :used]
+        table[b, used:used + 18] = free[18 * b:18 * b + 18]
+    st.table = table
+    st.upload(wq)
+    rope, ws = wq.rope_table(1000, D), wq.kv4_workspace(8, st.cache)
+    qkv = torch.empty((2 * n, 12, D), dtype=torch.bfloat16, device=dev())
+    side = torch.cuda.Stream()
+
+    def step(stream=None):
+        q = wq.kv4_append(st.cache, st.batch, qkv[:, 8:10], qkv[:, 10:], Q=qkv[:, :8], rope=rope, stream=stream)
+        return q, wq.kv4_attention(q, st.cache, st.batch, workspace=ws, stream=stream)
+
+    def new_tokens(seed):
+        x = kv4_ref.bf16(np.random.default_rng(seed).normal(size=(2 * n, 12, D)))
+        qkv.copy_(bf16_to_dev(x).view_as(qkv))
+        torch.cuda.synchronize()
+
+    def verify(q, O):
+        torch.cuda.synchronize()
+        st.pool = st.cache.pool.cpu().numpy()
+        st.check(kv4_ref.bf16(q.float().cpu().numpy()), O, 8, D ** -0.5, many_rows=True)
+
+    new_tokens(1)
+    verify(*step(side))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, O = step()
+    for i in range(2):
+        st.kv = [m + n for m in st.kv]
+        st.batch.kv_len.copy_(_i32(st.kv))
+        new_tokens(2 + i)
+        graph.replay()
+        verify(q, O)
+
+
+@pytest.mark.parametrize("D,n", MANY)
+def test_more_sequences_than_threads(wq, D, n):  # noqa: F811
+    """700 ragged sequences, some without new tokens, the longest with the block that picks this kernel."""
+    rng = np.random.default_rng(85)
+    q = rng.integers(0, 3, size=700).tolist()
+    kv = [max(int(rng.integers(1, 40)), m) for m in q]
+    q[411], kv[411] = n, 2000
+    q[699], kv[699] = n // 2, 130
+    st = Step(wq, q, kv, D=D, group=32, page=16, Hkv=1, seed=86)
+    bits, O = _attend(wq, st, Hq=4)
+    st.check(bits, O, 4, D ** -0.5, many_rows=True)
