@@ -287,7 +287,8 @@ typedef struct {
    not fit (cu_q not ascending within [0, num_tokens], kv_len outside [0,
    max_pages * page_size]) are clamped and recorded as WQ_ERR_DEVICE_BOUNDS,
    as are pages outside [0, num_pages).  Tokens past cu_q[num_seqs] belong to
-   no sequence: nothing of them is read or written (a step captured for more
+   no sequence: nothing of them is written, and what their rows hold is not
+   used (the rows are there, as all num_tokens are; a step captured for more
    tokens than it has needs no second graph). */
 typedef struct {
   const int32_t* page_table; /* [num_seqs][max_pages] */
@@ -339,7 +340,8 @@ WQ_API void wq_debug_kv4_seventh(const float* in, float* out, int64_t n);
  *   positions  int32 [num_tokens] rows of `rope`, or NULL: the slot index
  *   rot_dim    leading dimensions that are rotated, a multiple of 16 up to D:
  *              pairs (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved
- * A pair (a, b) becomes (a c - b s, a s + b c).  A rotated key is the exact
+ * A pair (a, b) becomes (a c - b s, a s + b c).  A rotated query is computed in
+ * fp32 (two roundings) and rounded to bf16.  A rotated key is the exact
  * value rounded once to fp32, x; then s = bf16(max|x| / 7) over its group (1
  * where that is 0) and q = clamp(rint(x / s), -8, 7), divisions in IEEE
  * fp32, ties to even.  A group with a NaN or an infinity gets the scale NaN

@@ -436,7 +436,8 @@ token_logprobs_kernel(const Params p) {
       if (round + 1 == again && round + 1 < rounds) {  // (uniform)
         again *= 2;
         if (k > 1) {
-          // the k-th best of all lists; a warp's lanes from k on are empty
+          // the k-th best of all lists (lanes from k on hold keys that were pushed
+          // out of their list, or none: the bound is as true with them)
           s_lane[tid] = static_cast<uint32_t>(st.mine >> 32);
           __syncthreads();
           kth_of_lanes();
