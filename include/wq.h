@@ -383,7 +383,7 @@ WQ_API size_t wq_kv4_workspace_bytes(int64_t Hq, int Hkv, int D);
  * with fp32 scores, softmax statistics and sums; a weight times its value's
  * scale (or the power of two below it) is rounded to fp16 (11 significant
  * bits, for products down to 2^-20 of the row's largest), O once to bf16.
- * Where a sequence has more than 16 rows (tokens times Hq / Hkv; 64 where D is
+ * Where a sequence has more than 32 rows (tokens times Hq / Hkv; 64 where D is
  * 64; D 256 has no such kernel) the scales of one key or value are held relative
  * to the largest of them, in fp16: those below 2^-17 of it lose bits.  Query head h reads key/value head
  * h / (Hq / Hkv).  A value scale of NaN makes the rows that see it NaN, in its

@@ -1,4 +1,4 @@
-"""The many-row attention over the 4-bit cache (more than 16 rows of a head of 128
+"""The many-row attention over the 4-bit cache (more than 32 rows of a head of 128
 and sequence, or 64 of a head of 64) where its own paths can go wrong."""
 import numpy as np
 import pytest

@@ -13,7 +13,7 @@
 // operations make two operands.
 //
 //  * Rows.  The query rows of one key/value head (tokens x grouped heads) in
-//    tiles of 8 or 16 (8 NT).  Both products run transposed, on m16n8k16 with
+//    tiles of 8, or 16 for heads of 64 (8 NT).  Both products run transposed, on m16n8k16 with
 //    n = 8 query rows: S^T = K Q^T (m = 16 keys), then O^T = V^T P^T (m = 16
 //    dimensions, k = 16 keys), so eight rows waste nothing; the weights become
 //    the second product's operand by an 8 x 8 transpose within the warp.

@@ -6,38 +6,44 @@ namespace wq {
 cudaError_t launch_kv4_split_d128(const Kv4Args& a, const Kv4AttentionArgs& x, cudaStream_t stream) {
   using namespace kv4split;
   const int G = a.D / a.group;
-  // A tile of 8 rows where no sequence has more, else 16: one tile of 16
-  // reads the codes once where two of 8 read them twice.
-  const bool small = a.max_q * (x.Hq / a.Hkv) <= 8;
-  if (G == 1) return small ? launch_variant<128, 1, 1>(a, x, stream) : launch_variant<128, 1, 2>(a, x, stream);
-  if (G == 2) return small ? launch_variant<128, 2, 1>(a, x, stream) : launch_variant<128, 2, 2>(a, x, stream);
-  if (G == 4) return small ? launch_variant<128, 4, 1>(a, x, stream) : launch_variant<128, 4, 2>(a, x, stream);
+  // Tiles of 8 rows only: the accumulators of 16 rows of 128 dimensions do not fit a
+  // thread's 128 registers beside the rest.  (16 rows in one tile of 16, spilled,
+  // against two of 8, which read the codes twice, us: 64 sequences of 4096 230 / 129; 8
+  // of 16384 119 / 72; 8 of 1024 26 / 21; one of 131071 129 / 71.)
+  if (G == 1) return launch_variant<128, 1, 1>(a, x, stream);
+  if (G == 2) return launch_variant<128, 2, 1>(a, x, stream);
+  if (G == 4) return launch_variant<128, 4, 1>(a, x, stream);
   return cudaErrorNotSupported;
 }
 
 size_t kv4_workspace_bytes(int D, int num_sms) {
   using namespace kv4split;
-  // partial rows: two slots for each CTA of the few-row kernel (16 rows), or of the many-row kernel (one, 256 rows)
+  // partial rows: two slots for each CTA of the few-row kernel (16 rows at most), or of the many-row kernel (one, 256 rows)
   const size_t few = static_cast<size_t>(2 * kMaxCtasSm) * num_sms * kMaxRows, many = D == 256 ? 0 : static_cast<size_t>(2) * num_sms * 256;
   return kv4_counter_bytes(num_sms) + (few > many ? few : many) * (D + 4) * 4;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Args& a, const Kv4AttentionArgs& x, cudaStream_t stream) {
-  // More than 16 rows of a head and sequence (64, for heads of 64) go to the many-row
+  // More than 32 rows of a head and sequence (64, for heads of 64) go to the many-row
   // kernel, which reads the codes once for up to 256 rows where this one reads them
-  // once for 16.  Heads of 128 (32 query and 8 key/value heads), us at 32 / 64 / 128
-  // rows, few-row kernel against many-row: 8 sequences of 16384: 223 / 424 / 826
-  // against 122 / 126 / 140; 32 of 4096: 217 / 415 / 834 against 138 / 144 / 161; 8 of
-  // 1024: 31 / 46 / 65 against 40 / 46 / 55; one of 16384: 46 / 63 / 98 against 46 / 60
-  // / 89; 16 rows 119 against 20 rows 125.  (Of a few short sequences the few-row
-  // kernel does better up to 64 rows, by 10 us; how long they are is not known here.)
-  // Heads of 64, at 32 / 48 / 64 rows: 8 of 16384: 66 / 90 / 113 against 108 / 108 /
-  // 108; 32 of 4096: 68 / 93 / 120 against 118 / 118 / 119; 8 of 1024: 21 / 23 / 28
-  // against 34 / 34 / 35; one of 16384: 27 / 24 / 31 against 42 / 43 / 43: the many-row
-  // kernel's chain for a block hardly shrinks with the dimensions.
+  // once for 8 (or 16).  us, few-row kernel / many-row, 32 query and 8 key/value heads:
+  //   heads of 128, rows     24           32           40
+  //   8 sequences of 16384   99 / 125     123 / 122    150 / 130
+  //   64 of 4096             184 / 258    240 / 258    292 / 268
+  //   8 of 1024              22 / 39      23 / 39      25 / 43
+  //   one of 131071          101 / 139    119 / 128    149 / 162
+  //   (group 32: 32 rows 141 / 128, 275 / 270, 25 / 39, 136 / 132)
+  //   heads of 64, rows      32           48           64
+  //   8 sequences of 16384   66 / 108     90 / 108     113 / 108
+  //   32 of 4096             68 / 118     93 / 118     120 / 119
+  //   8 of 1024              21 / 34      23 / 34      28 / 35
+  //   one of 16384           27 / 42      24 / 43      31 / 43
+  // (The many-row kernel's chain for a block hardly shrinks with rows or dimensions.)
+  // A few short sequences, or one, do better here with more rows too; how long they
+  // are is not known to the host.
   const int64_t rows = a.max_q * (x.Hq / a.Hkv);  // of one head of a sequence, at most
   if (a.D == 64 && rows > 64) return launch_kv4_tile_d64(a, x, stream);
-  if (a.D == 128 && rows > 16) return launch_kv4_tile_d128(a, x, stream);
+  if (a.D == 128 && rows > 32) return launch_kv4_tile_d128(a, x, stream);
   if (a.D == 64) return launch_kv4_split_d64(a, x, stream);
   if (a.D == 128) return launch_kv4_split_d128(a, x, stream);
   return launch_kv4_split_d256(a, x, stream);
