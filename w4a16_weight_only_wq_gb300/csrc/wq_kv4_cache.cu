@@ -25,9 +25,11 @@
 //
 // Measured (32 query and 8 key/value heads of 128): 8192 tokens: 63 us, 2.8 TB/s;
 // 40 of them keys and values, about 500 instructions for two rows of 128 (the exact
-// rotation, the codes, their transposition): the issue slots are 68% taken.  One token
-// 5.1 us: a launch, the sequence's lookup and one row.  Reading back: 8192 tokens
-// 16 us, 2.6 TB/s, one 3.1 us.
+// rotation, the codes, their transposition): 64% of the issue slots are taken while
+// 41% of an SM's warps are resident, and a token's lookup and loads are waited for in
+// the rest.  (Interleaved pairs 55 us; heads of 64: 43, of 256: 100.)  One token 5.1 us:
+// a launch, the sequence's lookup and one row.  Reading back: 8192 tokens 16 us, 2.6
+// TB/s (heads of 64: 12, of 256: 31), one 3.1 us.
 #include "wq_device.cuh"
 #include "wq_kv4.cuh"
 

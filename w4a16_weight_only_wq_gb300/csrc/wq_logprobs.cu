@@ -19,7 +19,8 @@
 // Measured (bf16 but where said): 4096 x 248000, k = 1: 348 us, 5.8 TB/s, 84% of
 // the issue slots (k = 0 307, 6.6 TB/s); 128 x 131071, k = 5: 23 us, 1.5 TB/s (k = 0 14: a launch, the
 // first loads and the joins of three segments a row; the lists take the rest);
-// 16 x 248000, k = 20: 16.5 us (k = 0 8.6); 1 x 32000 fp32, k = 0: 5.3 us.
+// 16 x 248000, k = 20: 16.5 us (k = 0 8.6); 1 x 32000 fp32, k = 0: 5.3 us; 2048 x 131071
+// fp32: k = 0 166, 6.5 TB/s, k = 1 179, k = 5 211 (bf16 93, 114, 147).
 //
 // Alternatives: each warp keeps its k best in order, one a lane, as 64-bit
 // keys (the logit's ordered bits, then the id's complement, so that equal
